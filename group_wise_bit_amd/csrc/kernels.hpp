@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "fp8_plan.hpp"
+
 namespace gwb {
 
 constexpr int kF32 = 0;   // gwb_dtype values
@@ -226,15 +228,6 @@ struct GemmArgs {
   int K;
   bool vec;                            // y takes stores of 4 elements
 };
-// The kernel of a shape, its K splits and its threads in all (exact: float32 outputs).
-struct GemmPlan {
-  int kernel, splits;
-  int64_t threads;
-};
-enum { kRows8, kRows8Deep, kRows8Narrow, kRows16, kRows16Deep, kRows16Narrow, kRows32, kRows32Deep, kRows32Narrow,
-       kTile64, kTile64x128, kTile64x192, kTile128, kTile128Deep, kTile128x192, kTile256x192, kTile256 };
-GemmPlan fp8_gemm_plan(int64_t M, int64_t N, int64_t K, bool exact);
-size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);   // the splits' float32 partial sums
 void launch_fp8_gemm(const GemmArgs& g, bool e8m0, int32_t y_dtype, hipStream_t st);
 
 // ---- measurement copy (common.hip)
