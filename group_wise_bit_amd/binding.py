@@ -658,8 +658,11 @@ def _fp8_gemm_args(x, w, y_dtype, out, workspace):
     if workspace is None:
         nb = fp8_gemm_workspace_bytes(M, N, K)
         workspace = _alloc(nb, out.device) if nb else None
-    return out, workspace, (ctypes.byref(tx), M, ctypes.byref(tw), N, K, yp, _DT[out.dtype], ldy, _ptr(workspace),
-                            0 if workspace is None else workspace.numel(), _stream())
+    elif not workspace.is_cuda or workspace.get_device() != out.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on x's device")
+    ws_b = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return out, workspace, (ctypes.byref(tx), M, ctypes.byref(tw), N, K, yp, _DT[out.dtype], ldy, _ptr(workspace), ws_b,
+                            _stream())
 
 
 def fp8_gemm(x: Fp8, w: Fp8, y_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
