@@ -528,10 +528,14 @@ def fp8_empty(R: int, K: int, block_rows: int = 1, scale: str = "f32", device="c
 
 
 def _rows_args(what: str, t: torch.Tensor, shape, like: Optional[torch.Tensor] = None):
-    """(pointer, row stride) of a row-major CUDA tensor of this shape, with `like`'s type and device."""
+    """(pointer, row stride) of a row-major CUDA tensor of this shape, with `like`'s type and device
+    (without one: on the current device)."""
     if t.shape != shape or t.dtype not in _DT or not t.is_cuda:
         raise ValueError(f"{what} must be a float32, bfloat16 or float16 CUDA tensor {tuple(shape)}")
-    if like is not None and (t.dtype != like.dtype or t.get_device() != like.get_device()):
+    if like is None:
+        if t.get_device() != _device():                 # calls run there, on its current stream
+            raise ValueError(f"{what} must be on the current device, {_device()}")
+    elif t.dtype != like.dtype or t.get_device() != like.get_device():
         raise ValueError(f"{what} must have the type and device of x")
     ld, s1 = t.stride()
     R, K = shape

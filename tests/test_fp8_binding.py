@@ -93,3 +93,28 @@ def test_gemm_workspace_is_counted_in_bytes():
         ws = Tensor((need // dt.itemsize,), dt)
         _, _, args = gwb._fp8_gemm_args(fp8(M, K), fp8(N, K, 128), None, Tensor((M, N)), ws)
         assert args[8] == ws.data_ptr() and args[9] == need
+
+
+CALLS = {
+    "quantize": lambda d: gwb.fp8_quantize(Tensor((8, 256), dev=d), out=fp8(8, 256, dev=d)),
+    "prepare_quantize": lambda d: gwb.prepare_fp8_quantize(Tensor((8, 256), dev=d), fp8(8, 256, dev=d)),
+    "rmsnorm": lambda d: gwb.rmsnorm_fp8(Tensor((8, 256), dev=d), out=fp8(8, 256, dev=d)),
+    "prepare_rmsnorm": lambda d: gwb.prepare_rmsnorm_fp8(Tensor((8, 256), dev=d), None, 1e-6, None, fp8(8, 256, dev=d), None),
+    "silu_mul": lambda d: gwb.silu_mul_fp8(Tensor((8, 512), dev=d), out=fp8(8, 256, dev=d)),
+    "prepare_silu_mul": lambda d: gwb.prepare_silu_mul_fp8(Tensor((8, 512), dev=d), fp8(8, 256, dev=d)),
+    "gemm": lambda d: gwb.fp8_gemm(fp8(8, 256, dev=d), fp8(16, 256, 128, dev=d), out=Tensor((8, 16), dev=d)),
+    "prepare_gemm": lambda d: gwb.prepare_fp8_gemm(fp8(8, 256, dev=d), fp8(16, 256, 128, dev=d), Tensor((8, 16), dev=d)),
+}
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_tensors_of_another_device_are_refused(name):
+    """Calls run on the current device and its stream: tensors of another one would be read
+    there, in no order with what wrote them."""
+    with pytest.raises(ValueError, match="current"):
+        CALLS[name](1)
+    if name.startswith("prepare"):
+        CALLS[name](0)                                    # the same on the current device is accepted
+    else:
+        with pytest.raises(AssertionError, match="reached"):
+            CALLS[name](0)
