@@ -1,10 +1,13 @@
 """The plan of the FP8 product (csrc/fp8_plan.hpp, host arithmetic) compiled with the host
 compiler and swept over shapes: every launch it leads to has work."""
 import os
+import re
 import shutil
 import subprocess
 
 import pytest
+
+import _fp8_shapes
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "group_wise_bit_amd", "csrc")
@@ -50,3 +53,36 @@ def test_every_launch_has_work(tmp_path):
     subprocess.run([CXX, "-std=c++17", "-O2", "-I", CSRC, str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+PRINT = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "fp8_plan.hpp"
+int main(int argc, char** argv) {
+  for (int i = 1; i + 2 < argc; i += 3) {
+    const gwb::GemmPlan p = gwb::fp8_gemm_plan(atol(argv[i]), atol(argv[i + 1]), atol(argv[i + 2]), false);
+    printf("%d %d %d\n", p.kernel, p.splits > 1, p.wide < atol(argv[i + 1]));
+  }
+}
+"""
+
+
+@pytest.mark.skipif(CXX is None, reason="no host C++ compiler")
+def test_the_shapes_of_the_gpu_tests_reach_every_kernel(tmp_path):
+    src, exe = tmp_path / "plan.cpp", tmp_path / "plan"
+    src.write_text(PRINT)
+    subprocess.run([CXX, "-std=c++17", "-O1", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    text = open(os.path.join(CSRC, "fp8_plan.hpp")).read()
+    names = re.search(r"enum \{([^}]*)\}", text).group(1).replace("\n", " ").replace(" ", "").split(",")
+    for table in (_fp8_shapes.SHAPES, _fp8_shapes.LONG):
+        args = [str(v) for shape in table.values() for v in shape]
+        out = subprocess.run([str(exe), *args], capture_output=True, text=True, check=True).stdout.split("\n")
+        got = []
+        for line in out[:-1]:
+            kernel, split, tail = map(int, line.split())
+            got.append(names[kernel] + (" split" if split else "") + (" tail" if tail else ""))
+        assert got == list(table)
+    assert {n.split()[0] for n in _fp8_shapes.SHAPES} == set(names)
+    assert {n.split()[0] for n in _fp8_shapes.LONG} == {n for n in names if n.startswith("kTile")}
+    assert all((k + 127) // 128 > 64 for _, _, k in _fp8_shapes.LONG.values())
