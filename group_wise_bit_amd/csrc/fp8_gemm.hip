@@ -8,9 +8,13 @@
 // Precision. The FP8 matrix cores add the products of 8 adjacent k (8 bytes of a lane)
 // after dropping bits below 2^-13 of the largest of them (measured: a product 2^-14 times
 // its neighbour's vanishes, in another group of 8 it counts down to 2^-23); the sums of
-// the groups and the accumulator are float32. On normal data that is 1.5e-5 of the result
-// (2-norm), under the rounding of a bf16 (2e-3) or float16 (2e-4) output, and it buys twice
-// the rate. For float32 outputs, EXACT: the codes are widened to bf16 (exactly, the scaled
+// the groups and the accumulator are float32. What goes depends on how unequal the 8
+// products are: of the result's 2-norm 2e-5 on normal data, 3e-5 to 7e-5 with 1 % of the
+// channels 20 times larger, 6e-5 to 8e-5 with them 200 times larger; at worst 7 * 2^-13 of
+// each group's largest product. Next to the rounding of a bf16 output (1.7e-3) that does not
+// show; the error of a float16 one (2.1e-4) grows by 0.5, 1 to 3 and 4 to 7 %. It buys twice
+// the rate, so 16-bit outputs take it; who wants float32 sums asks for a float32 output and
+// rounds that. For these, EXACT: the codes are widened to bf16 (exactly, the scaled
 // FP8 conversion at scale 1) and multiplied by v_mfma_f32_16x16x32_bf16, whose products
 // are exact and whose sums are float32.
 //

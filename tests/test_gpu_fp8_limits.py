@@ -66,6 +66,54 @@ def test_gemm_more_tile_rows_than_units(M, N, K, scale):
     _check_gemm(M, N, K, scale, (torch.bfloat16, torch.float16))
 
 
+# ------------------------------------------------------------------ precision
+def _dropped(x, w, rows, cols):
+    """2-norm, relative to the exact products of these rows and columns, of what the FP8 matrix
+    instructions may drop from them: within 8 adjacent k the bits of a product below 2^-13 of
+    the largest's power of two."""
+    xc, wc = x.codes[rows].double(), w.codes[cols].double()
+    xs, ws = _values64(x)[rows], _values64(w)[cols]
+    lost, ref = 0.0, xs @ ws.t().contiguous()
+    scale = torch.where(xc == 0, 0.0, xs / torch.where(xc == 0, 1.0, xc)), torch.where(wc == 0, 0.0, ws / torch.where(wc == 0, 1.0, wc))
+    K = xc.shape[1]
+    for k in range(0, K, 2048):
+        p = xc[:, None, k:k + 2048] * wc[None, :, k:k + 2048]
+        g = p.unflatten(2, (-1, 8))
+        q = torch.exp2(torch.floor(torch.log2(g.abs().amax(3, keepdim=True).clamp(min=2.0 ** -18))) - 13)
+        d = (g - torch.trunc(g / q) * q).flatten(2)
+        lost = lost + (d * scale[0][:, None, k:k + 2048] * scale[1][None, :, k:k + 2048]).sum(2)
+    return float(lost.norm() / ref.norm())
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("outlier", [1.0, 20.0])
+@pytest.mark.parametrize("M,N,K", _sorted(SHAPES) + [pytest.param(*v, id=k + " long K") for k, v in LONG.items()])
+def test_gemm_error_of_the_whole_and_of_each_row(M, N, K, outlier, scale):
+    """The 2-norm of the error against the 64-bit product: the rounding to the output type, which
+    is computed, and d, what the matrix instructions drop (float32 outputs: d = 0), formed on
+    1024 sampled outputs by the rule; the two are independent. Slack: d is known to some 20 %
+    from its sample, the sum to 2 % (5 rows of 199); a row of 199 outputs or more to 40 % with a
+    d of up to 3 times the mean. float32 sums: below 2^-20 (their bound, U (132 + KB) of the sum of
+    magnitudes, met by random signs). A product left out anywhere shows in its row:
+    1 / sqrt(K N) of the row's norm, which is 1.4 times the rounding of float16 at K N = 1e7."""
+    x, w = _operands(M, N, K, scale, M + N + K, outlier)
+    ref = _values64(x) @ _values64(w).t().contiguous()
+    g = torch.Generator().manual_seed(K)
+    rows, cols = torch.randint(0, M, (16,), generator=g).to(DEV), torch.randint(0, N, (64,), generator=g).to(DEV)
+    drop = _dropped(x, w, rows, cols)
+    for dt in DTYPES:
+        err = gwb.fp8_gemm(x, w, dt).double() - ref
+        r = ref.to(dt).double() - ref
+        d = 0.0 if dt == torch.float32 else drop
+        whole = float(err.norm() / ref.norm())
+        bound = 1.02 * ((float(r.norm() / ref.norm())) ** 2 + (1.2 * d) ** 2) ** 0.5 + 2.0 ** -20
+        print(f"{dt} {scale}: error {whole:.3g}, rounding {float(r.norm() / ref.norm()):.3g}, dropped {d:.3g}")
+        assert whole <= bound, (dt, whole, bound)
+        n = ref.norm(dim=1)
+        by_row = 1.4 * ((r.norm(dim=1)) ** 2 + (3 * d * n) ** 2).sqrt() + 2.0 ** -19 * n
+        assert bool((err.norm(dim=1) <= by_row).all()), (dt, float((err.norm(dim=1) / by_row).max()))
+
+
 # ------------------------------------------------------------------ surroundings
 @pytest.mark.parametrize("scale", ["f32", "e8m0"])
 @pytest.mark.parametrize("M,N,K", _sorted(SHAPES))
