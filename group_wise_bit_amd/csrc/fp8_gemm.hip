@@ -3,7 +3,10 @@
 //   P_kb[m, n] = sum over the block's k of x[m, k] * w[n, k],
 // with x in 1 x 128 blocks and w in 128 x 128 blocks. One v_mfma_f32_16x16x128_f8f6f4
 // forms a 16 x 16 tile of P_kb: its 128 k are exactly one scale block, so the scales
-// (float32) enter with one float32 product and fused multiply-add per output and block.
+// (float32) enter with one float32 product and fused multiply-add per output and block; in
+// tiles of 16-bit outputs, E8M0 scales enter in the instruction itself. The two agree while
+// the product of the scales is a normal float32; beyond, the second keeps what the first
+// rounds to 0 or infinity.
 //
 // Precision. The FP8 matrix cores add the products of 8 adjacent k (8 bytes of a lane)
 // after dropping bits below 2^-13 of the largest of them (measured: a product 2^-14 times

@@ -382,8 +382,8 @@ int gwb_silu_mul_fp8(const void* gate_up, int32_t dtype, int64_t M, int64_t I, i
                      void* stream);
 
 /* y[m, n] = sum_k x[m, k] * w[n, k] of two block-scaled matrices, on the FP8 matrix cores:
- * per block of 128 k the products of the codes are summed (below), the sum multiplied by
- * the float32 product of the two scales and added in float32.
+ * per block of 128 k the products of the codes are summed, the sum multiplied by the two
+ * scales and added in float32 (how: below).
  *   x  block_rows 1, [M, K];  w  block_rows 128, [N, K]; scales of one type (else
  *      GWB_E_UNSUPPORTED); K % 16 == 0 (else GWB_E_SHAPE); codes and their strides 16-byte
  *      aligned, strides at most 2^23; M, N and K below 2^30 (else GWB_E_UNSUPPORTED)
@@ -396,7 +396,12 @@ int gwb_silu_mul_fp8(const void* gate_up, int32_t dtype, int64_t M, int64_t I, i
  * product: of the result's 2-norm 2e-5 on normal data and up to 7e-5 with 1 % of the
  * channels 20 times larger, at worst 7 * 2^-13 of each 8's largest product. A float16
  * output's error (2.1e-4 of rounding) grows by 0.5 % and 1 to 3 % there, a bf16 one's
- * (1.7e-3) not noticeably. A float32 output, rounded by the caller, avoids it.        */
+ * (1.7e-3) not noticeably. A float32 output, rounded by the caller, avoids it.
+ * Scales: the product of the two scales of a block is to be below 2^128, and at least 2^-126
+ * where the block's sum is not zero. Beyond that results depend on M: with E8M0 scales and
+ * a 16-bit output the kernels for many rows apply both exponents exactly, all others form
+ * the product as a float32, which loses bits or is 0, or infinite (NaN with a sum of 0).
+ * A NaN scale makes NaN of every output of its row, or of its 128 columns.             */
 int gwb_fp8_gemm_workspace(int64_t M, int64_t N, int64_t K, size_t* bytes);
 int gwb_fp8_gemm(const gwb_fp8* x, int64_t M, const gwb_fp8* w, int64_t N, int64_t K, void* y, int32_t y_dtype,
                  int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);

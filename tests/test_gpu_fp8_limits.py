@@ -144,3 +144,79 @@ def test_gemm_strides_and_surroundings(M, N, K, scale):
             assert torch.equal(y, want), (dt, pad, off)
             y.fill_(9.0)
             assert bool((buf == 9.0).all()), (dt, pad, off)
+
+
+# ------------------------------------------------------------------ special codes and scales
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("M,N,K", _sorted(SHAPES))
+def test_gemm_nan_code_stays_in_its_row_and_column(M, N, K, scale):
+    x, w = _operands(M, N, K, scale, M + 2 * N)
+    clean = [gwb.fp8_gemm(x, w, dt) for dt in DTYPES]
+    x.codes.view(torch.uint8)[2, K - 6] = 0x7F             # in the last, short stage
+    w.codes.view(torch.uint8)[N - 2, K - 3] = 0xFF
+    w.codes.view(torch.uint8)[77, 3] = 0xFF
+    nan = torch.zeros(M, N, dtype=torch.bool, device=DEV)
+    nan[2], nan[:, 77], nan[:, N - 2] = True, True, True
+    for dt, y0 in zip(DTYPES, clean):
+        y = gwb.fp8_gemm(x, w, dt)
+        assert torch.equal(torch.isnan(y), nan), dt
+        assert torch.equal(y.masked_fill(nan, 0), y0.masked_fill(nan, 0)), dt
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("M,N,K", _sorted(SHAPES))
+def test_gemm_every_scale_byte(M, N, K, scale):
+    """Scales 2^-127 to 2^127 and NaN on the weight's blocks, all codes 1, x with one 1 per row:
+    each output is one scale, rounded to its type (a bf16 or float32 below 2^-126 may be 0), and
+    NaN in the row blocks that have a NaN scale: 0 * NaN."""
+    nb, kb = -(-N // 128), -(-K // 128)
+    wc = torch.full((N, K), 0x38, dtype=torch.uint8, device=DEV).view(E4M3)
+    xc = torch.zeros(M, K, dtype=torch.uint8, device=DEV)
+    rows = torch.arange(M, device=DEV)
+    col = (rows * 7) % kb                                  # the row's column block
+    xc[rows, (col * 128 + rows % 128).clamp(max=K - 1)] = 0x38
+    x = gwb.Fp8(xc.view(E4M3), _byte_scales(torch.full((kb, M), 127, device=DEV), scale), 1)
+    row_block = torch.arange(N, device=DEV) // 128
+    for first in range(0, 256, nb * kb):
+        b = (torch.arange(nb * kb, device=DEV) + first).view(nb, kb) % 256
+        w = gwb.Fp8(wc, _byte_scales(b, scale), 128)
+        want = torch.exp2(b[row_block][:, col].t().double() - 127)
+        want = want.masked_fill((b == 255).any(1)[row_block][None, :], torch.nan)
+        for dt in DTYPES:
+            y = gwb.fp8_gemm(x, w, dt)
+            same = torch.isclose(y.double(), want.to(dt).double(), rtol=0, atol=2.0 ** -126, equal_nan=True)
+            assert bool(same.all()), (dt, first)
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("M,N,K", _sorted(SHAPES))
+def test_gemm_scale_products_over_their_range(M, N, K, scale):
+    """One code of x per row against random codes, the scales' product from 2^-126 to 2^127 (the range the
+    header states): with codes of 1 each output is exactly the product, rounded to its type; with
+    random codes, away from the ends, code * product. The kernels for few and for many rows agree."""
+    g = torch.Generator(device=DEV).manual_seed(N + K)
+    nb, kb = -(-N // 128), -(-K // 128)
+    rows = torch.arange(M, device=DEV)
+    col = (rows * 5) % kb
+    at = (col * 128 + rows * 3 % 128).clamp(max=K - 1)
+    col = at // 128
+    xc = torch.zeros(M, K, dtype=torch.uint8, device=DEV)
+    xc[rows, at] = 0x38
+    row_block = torch.arange(N, device=DEV) // 128
+    for lo, hi, random_codes in ((64, 191, False), (100, 154, True)):
+        bx = torch.randint(lo, min(hi, 190) + 1, (kb, M), generator=g, device=DEV)
+        bw = torch.randint(lo, hi + 1, (nb, kb), generator=g, device=DEV)
+        bx[col[0], 0], bw[0, col[0]] = lo, lo                # the ends themselves
+        bx[col[1], 1], bw[-1, col[1]] = min(hi, 190), hi
+        wc = torch.full((N, K), 0x38, dtype=torch.uint8, device=DEV)
+        if random_codes:
+            wc = torch.randint(0, 127, (N, K), generator=g, device=DEV).to(torch.uint8)
+            wc |= (torch.randint(0, 2, (N, K), generator=g, device=DEV) * 128).to(torch.uint8)
+        x = gwb.Fp8(xc.view(E4M3), _byte_scales(bx, scale), 1)
+        w = gwb.Fp8(wc.view(E4M3), _byte_scales(bw, scale), 128)
+        e = bx[col, rows][:, None] + bw[row_block][:, col].t() - 254
+        want = torch.exp2(e.double()) * wc.view(E4M3).double()[:, at].t()
+        for dt in DTYPES:
+            y = gwb.fp8_gemm(x, w, dt).double()
+            bad = y != want.to(torch.float32).to(dt).double()
+            assert not bool(bad.any()), (dt, random_codes, y[bad][:4], want[bad][:4], int(bad.sum()))
