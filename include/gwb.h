@@ -376,8 +376,8 @@ int gwb_rmsnorm_fp8(const void* x, int32_t dtype, int64_t M, int64_t K, int64_t 
                     int64_t ldy, const gwb_fp8* out, void* stream);
 
 /* gate_up [M, 2I] of dtype, gate in the first I columns (row stride ldg) ->
- * out = gate / (1 + exp(-gate)) * up (float32, to about 6 ulp; SiLU of a gate below -87 is
- * taken as 0) quantized in 1 x 128 blocks, [M, I].                                   */
+ * out = gate / (1 + exp(-gate)) * up (float32: SiLU within 7 * 2^-24 relative, of a gate
+ * below -87, less than 2e-36, taken as 0) quantized in 1 x 128 blocks, [M, I].       */
 int gwb_silu_mul_fp8(const void* gate_up, int32_t dtype, int64_t M, int64_t I, int64_t ldg, const gwb_fp8* out,
                      void* stream);
 

@@ -220,3 +220,28 @@ def test_gemm_scale_products_over_their_range(M, N, K, scale):
             y = gwb.fp8_gemm(x, w, dt).double()
             bad = y != want.to(torch.float32).to(dt).double()
             assert not bool(bad.any()), (dt, random_codes, y[bad][:4], want[bad][:4], int(bad.sum()))
+
+
+# ------------------------------------------------------------------ SiLU
+def test_silu_of_dense_gates():
+    """Every block has one gate, up = 2^40 (exact): the scale shows the value in float32. SiLU as
+    fp8.hpp forms it, u = 2^-24: 2^t to 1 ulp (2 u), its correction and the product u each, 1 + e^-g
+    one more: 5 u; the reciprocal with its Newton step u, the product with g u: 7 u; the scale's
+    quotient by 448 u. Together 8 u and second orders."""
+    gates = np.concatenate([np.linspace(-87, 88, 150001), np.linspace(-1, 1, 40001),
+                            np.ldexp(1.0, -np.arange(1, 90)), -np.ldexp(1.0, -np.arange(1, 90)), [-87.0, 0.0]]).astype(np.float32)
+    per = 64                                               # blocks per row
+    n = -(-len(gates) // per) * per
+    g = np.zeros(n, np.float32)
+    g[:len(gates)] = gates
+    rows = n // per
+    gu = torch.zeros(rows, 2 * per * 128, device=DEV)
+    gu[:, :per * 128:128] = torch.from_numpy(g.reshape(rows, per)).to(DEV)
+    gu[:, per * 128:] = 2.0 ** 40
+    q = gwb.silu_mul_fp8(gu)
+    got = q.scales.t().double().cpu().numpy().reshape(-1)
+    v = np.abs(o8.silu_mul(np.stack([g.astype(np.float64), np.full(n, 2.0 ** 40)], 1))[:, 0])
+    want = np.maximum(v / 448, 2.0 ** -126)
+    err = np.abs(got - want) / want / U
+    print(f"largest error {err.max():.2f} u at gate {g[err.argmax()]}")
+    assert err.max() <= 8.01
