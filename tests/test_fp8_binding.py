@@ -1,5 +1,7 @@
 """What the Python binding of the FP8 operators refuses before it calls the library, on
 stand-ins for GPU tensors: no GPU is touched, and a call that reached the library would fail."""
+import ctypes
+
 import pytest
 import torch
 
@@ -118,3 +120,19 @@ def test_tensors_of_another_device_are_refused(name):
     else:
         with pytest.raises(AssertionError, match="reached"):
             CALLS[name](0)
+
+
+@pytest.mark.parametrize("M,N,K", [(64, 5120, 17408), (128, 5120, 5120), (40, 259, 2064)])
+def test_a_product_that_splits_k_refuses_a_small_workspace(M, N, K):
+    """In the library itself: these shapes do split, so the refusals are reached."""
+    real, fake = gwb.lib.real, 1 << 20
+    need = gwb.fp8_gemm_workspace_bytes(M, N, K)
+    assert need > 0 and need % (4 * M * N) == 0
+    x = gwb.Fp8Tensors(fake, fake, K, M, 1, 0)
+    w = gwb.Fp8Tensors(fake, fake, K, -(-K // 128), 128, 0)
+
+    def go(ws, nbytes):
+        return real.gwb_fp8_gemm(ctypes.byref(x), M, ctypes.byref(w), N, K, fake, gwb.BF16, N, ws, nbytes, None)
+    assert go(fake, need - 1) == gwb.E_SIZE
+    assert go(None, need) == gwb.E_SIZE
+    assert go(fake + 8, need) == gwb.E_UNSUPPORTED
