@@ -163,6 +163,9 @@ void launch_fp8_blocks(int32_t dtype, const void* w, int64_t ldw, int64_t N, int
 // float32 rows leave as two half-lines per lane: ordinary stores, which L2 joins, are
 // faster there (2048 x 5120 30 us against 34). Runs of 32 workgroups go to one XCD, so that
 // its L2 joins the neighbouring rows' 4-byte scales into lines (8192 x 2048: 24.4 -> 23.3 us).
+// 7 and 8 units per lane (beyond 49152 columns) do not fit the 128 registers that 1024 threads
+// leave a lane where rows are unaligned (up to 81 spilled) or, with 8, float32 (49): 256 x 65535
+// takes 60 us, 256 x 65536 29.
 constexpr int64_t kNormStream = 32 << 20;   // bytes of residual beyond which it is streamed
 template <typename T, bool ALIGNED, int U>
 __global__ __launch_bounds__(1024) void rmsnorm_fp8_kernel(NormArgs a, int wpr, bool stream) {
