@@ -165,6 +165,25 @@ def test_gemm_nan_code_stays_in_its_row_and_column(M, N, K, scale):
 
 @pytest.mark.parametrize("scale", ["f32", "e8m0"])
 @pytest.mark.parametrize("M,N,K", _sorted(SHAPES))
+def test_gemm_nan_scale_stays_in_its_row_and_columns(M, N, K, scale):
+    """NaN scales of one row of x (its last column block) and of one row block of w (its first)."""
+    x, w = _operands(M, N, K, scale, 2 * M + N)
+    clean = [gwb.fp8_gemm(x, w, dt) for dt in DTYPES]
+    for s, at in ((x.scales, (-1, 3)), (w.scales, (1, 0))):
+        if scale == "e8m0":
+            s.view(torch.uint8)[at] = 255
+        else:
+            s[at] = float("nan")
+    nan = torch.zeros(M, N, dtype=torch.bool, device=DEV)
+    nan[3], nan[:, 128:256] = True, True
+    for dt, y0 in zip(DTYPES, clean):
+        y = gwb.fp8_gemm(x, w, dt)
+        assert torch.equal(torch.isnan(y), nan), dt
+        assert torch.equal(y.masked_fill(nan, 0), y0.masked_fill(nan, 0)), dt
+
+
+@pytest.mark.parametrize("scale", ["f32", "e8m0"])
+@pytest.mark.parametrize("M,N,K", _sorted(SHAPES))
 def test_gemm_every_scale_byte(M, N, K, scale):
     """Scales 2^-127 to 2^127 and NaN on the weight's blocks, all codes 1, x with one 1 per row:
     each output is one scale, rounded to its type (a bf16 or float32 below 2^-126 may be 0), and
